@@ -538,6 +538,7 @@ struct Warp {
                 }
             }
         }
+        __syncwarp();  // key and mask are read: the next batch may take their place
     }
 
     // The list in batches of 32 entries, dealt out to the warps of all slices in turn (the

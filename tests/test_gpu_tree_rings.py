@@ -1,0 +1,79 @@
+"""GPU parity of sparse_attn_tree where one CTA walks a whole list: every ring of the kernels (rows
+staged, entries resolved) wraps many times.
+
+So many sequences run at once that no list is split over a cluster.  They are copies of three
+sequences: those three are held against the fp64 reference within test_gpu_tree's tolerances, all
+others have to repeat their bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import kv_ref as R
+from gpu_util import dev, lists_to_device, t_i32
+from test_gpu_tree import check, make_cache, random_tree, ssa
+
+pytestmark = pytest.mark.gpu
+
+# copies of the three sequences with which no list is split: clusters of two CTAs would have to
+# fit 378 times (148 SMs x 5 CTAs at most) or 114 times (one CTA an SM)
+FEW, MANY = 126, 38
+
+
+def run_copies(fmt, d, G, T, S, lengths, diags, verts, copies, depth=4, seed=0, edit=None, scale=None, q_edit=None):
+    m = ssa()
+    base, (kv, vv) = make_cache(fmt, 3, 1, S, d, seed, edit)
+    many = lambda t: None if t is None else t.repeat(copies, *[1] * (t.dim() - 1))
+    cache = m.KVCache.from_tensors(many(base.k), many(base.v), many(base.k_scale), many(base.v_scale), format=fmt)
+    lists = m.tree_lists(m.extend(*lists_to_device(diags, verts)[0], S), 1, depth=depth)
+    g = np.random.default_rng(seed + 7)
+    q = R.bf16(g.standard_normal((3, T, G, d)))
+    if q_edit:
+        q_edit(q)
+    par = random_tree(g, 3, T, depth)
+    scale = d ** -0.5 if scale is None else scale
+    tq = many(torch.from_numpy(q).to(dev()).bfloat16()).contiguous()
+    O, L = m.attn_tree(tq, cache, many(t_i32(lengths)), many(t_i32(par)), lists, scale=scale)
+    nodes = [T] * 3
+    ref = R.tree_attention(q, kv, vv, lengths, par, nodes, diags, verts, scale, [0] * G)
+    check(O[:3], L[:3], ref, nodes)
+    bits = lambda x, t: x.view(t).view(copies, 3, *x.shape[1:])
+    for x, t in ((O, torch.int16), (L, torch.int32)):
+        y = bits(x, t)
+        assert (y == y[:1]).all()
+    return O[:3], L[:3]
+
+
+def odd_groups(fmt, odd):
+    """Groups that the products of whole tiles cannot take, in the keys `odd`: tiny, all-zero and
+    (element 3's group of values) not finite in turn; for bf16 rows infinite values."""
+    g = np.random.default_rng(11)
+
+    def edit(i, c, e=None):
+        if fmt == "bf16":
+            if i == 1:
+                c[:, :, odd, 3] = np.inf
+            return
+        e[:, :, odd[0::3]] = g.integers(60, 112, e[:, :, odd[0::3]].shape)
+        e[:, :, odd[1::3]] = 16
+        c[:, :, odd[1::3]] = 0
+        if i == 1:
+            c[:, :, odd[2::3], :32] = 0
+            e[:, :, odd[2::3], 0] = 255
+    return edit
+
+
+# 8, 16 and 32 rows a KV head
+@pytest.mark.parametrize("T", [4, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_odd_groups_in_every_batch_of_a_long_list(fmt, d, T):
+    # head 0 retains even columns and the node itself, head 1 everything; the first sequence's own
+    # rows lie behind the odd ones, so its head 0 stays finite
+    S, lengths = 1300, [1280, 1001, 700]
+    D = [np.array([0], np.int32), np.arange(1250, dtype=np.int32)]
+    C = [np.arange(0, S - 40, 2, dtype=np.int32), np.zeros(0, np.int32)]
+    odd = np.arange(1, 1280, 6)
+    O, L = run_copies(fmt, d, 2, T, S, lengths, D, C, FEW, edit=odd_groups(fmt, odd), seed=T)
+    assert torch.isfinite(O[0, :, 0]).all() and torch.isfinite(L).all()
+    assert torch.isfinite(O[:, :, 1, 32:]).all() and not torch.isfinite(O[:, :, 1, 3]).any()
