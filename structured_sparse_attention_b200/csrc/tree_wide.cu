@@ -539,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                             for (int e = 0; e < 8; ++e)
                                 dot = fmaf(__uint_as_float(static_cast<uint32_t>(__ldg(q_row + 8 * c + e)) << 16), x.value(e), dot);
                         }
+                        __syncwarp();  // the loop ran in some lanes; tensor memory is read by the whole warp
                         const float y = in ? dot * p.scale_log2 : -INFINITY;
                         const float up = fmaxf(m, y), f = up == m ? 1.0f : ex2_approx(m - up);
                         const float wt = in ? ex2_approx(y - up) : 0.0f;
@@ -659,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t r[32];
+            __syncwarp();  // after the stores of some lanes: the whole warp reads its columns
             tmem_ld32(t_o + c, r);
             tmem_wait_ld();
             if (direct) {  // the only part: the result

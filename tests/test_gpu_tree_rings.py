@@ -77,3 +77,18 @@ def test_odd_groups_in_every_batch_of_a_long_list(fmt, d, T):
     O, L = run_copies(fmt, d, 2, T, S, lengths, D, C, FEW, edit=odd_groups(fmt, odd), seed=T)
     assert torch.isfinite(O[0, :, 0]).all() and torch.isfinite(L).all()
     assert torch.isfinite(O[:, :, 1, 32:]).all() and not torch.isfinite(O[:, :, 1, 3]).any()
+
+
+# 40 and 128 rows a KV head, and two blocks of rows
+@pytest.mark.parametrize("G,T", [(2, 20), (2, 64), (3, 50)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_odd_groups_in_every_tile_of_a_long_list(fmt, d, G, T):
+    # lists of more than 17 tiles of 64 keys; heads as above, a third one like the second
+    S, lengths = 1300, [1230, 1001, 700]
+    D = [np.array([0], np.int32)] + [np.arange(1250, dtype=np.int32)] * (G - 1)
+    C = [np.arange(0, S - 100, 2, dtype=np.int32)] + [np.zeros(0, np.int32)] * (G - 1)
+    odd = np.arange(1, 1200, 48)
+    O, L = run_copies(fmt, d, G, T, S, lengths, D, C, MANY, edit=odd_groups(fmt, odd), seed=T)
+    assert torch.isfinite(O[0, :, 0]).all() and torch.isfinite(L).all()
+    assert torch.isfinite(O[:, :, 1, 32:]).all() and not torch.isfinite(O[:, :, 1, 3]).any()

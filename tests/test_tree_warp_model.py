@@ -7,9 +7,13 @@ slot has to be read for the last time before such an instruction, and written ag
 after it.  The model runs the lanes in random order between those points, tags each slot with
 its batch, and fails on a read that finds another batch's entry."""
 
+import os
 import random
+import re
 
 import pytest
+
+from conftest import ROOT
 
 LANES = 32
 
@@ -97,13 +101,25 @@ def test_key_by_key_needs_a_barrier_at_its_end():
     run(0, 1, True, end_barrier=False)  # lists of one batch never reuse a slot
 
 
-def test_the_kernel_has_the_barrier():
-    import os
-    import re
+def source(name):
+    with open(os.path.join(ROOT, "structured_sparse_attention_b200", "csrc", name)) as f:
+        return f.read()
 
-    from conftest import ROOT
-    with open(os.path.join(ROOT, "structured_sparse_attention_b200", "csrc", "tree.cu")) as f:
-        src = f.read()
+
+def test_the_kernel_has_the_barrier():
+    src = source("tree.cu")
     body = src[src.index("void one_by_one("):]
     body = body[:body.index("\n    }\n")]
     assert re.search(r"__syncwarp\(\);[^\n]*$", body.rstrip()), "one_by_one must end in a warp barrier"
+
+
+def test_tensor_memory_is_read_by_whole_warps():
+    # attn_tree_wide_kernel: code that runs in some lanes of a warp (a loop under a lane's own
+    # condition, stores of the rows that exist) is followed by a warp barrier before the next
+    # access to tensor memory, which is an instruction of the whole warp
+    src = source("tree_wide.cu")
+    kernel = src[src.index("void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel"):]
+    loop = kernel.index("in && c < D / 8")
+    assert "__syncwarp();" in kernel[loop:kernel.index("tmem_ld8(", loop)]
+    last = kernel.index("const bool direct")
+    assert "__syncwarp();" in kernel[kernel.index("for (int c", last):kernel.index("tmem_ld32(", last)]
