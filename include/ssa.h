@@ -406,7 +406,10 @@ SSA_API int sparse_attn_decode(const void *Q, const void *K, const void *V, int 
  * (M = 448 or 6, the largest code), and it is a bf16 number exactly.  e lies in
  * [-111, 7] (e4m3) or [-111, 13] (e2m1), E = e + 127: larger values saturate at
  * 448 * 2^7 = 57344 or 6 * 2^13 = 49152.  A group that holds a NaN or an infinity is
- * stored as codes 0 with E = 255 and reads back as NaN. */
+ * stored as codes 0 with E = 255 and reads back as NaN.  A cache made elsewhere holds
+ * E from 16 to 134 (e4m3) or 140 (e2m1), 255 with codes 0, or 0 with codes 0 (a row never
+ * written).  An E above that in a row that a call reads sets SSA_ERR_INVALID in dev_status, and
+ * the row's values are unspecified; values of one from 1 to 15 may round to zero. */
 #define SSA_KV_BF16 0 /* bf16 rows, no scales */
 #define SSA_KV_E4M3 1 /* 8 bits: sign, 4 exponent, 3 mantissa bits, one byte an element */
 #define SSA_KV_E2M1 2 /* 4 bits: sign, 2 exponent, 1 mantissa bit, two to a byte, even element low */

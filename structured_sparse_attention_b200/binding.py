@@ -589,7 +589,9 @@ class KVCache:
 
     @classmethod
     def from_tensors(cls, k, v, k_scale=None, v_scale=None, *, format: str = "bf16"):
-        """A cache over tensors the caller holds (laid out as above; not copied)."""
+        """A cache over tensors the caller holds (laid out as above; not copied).  Scale bytes are 16
+        to 134 (e4m3) or 140 (e2m1), 255 with codes 0 (NaN) or 0 with codes 0; a call that reads a
+        larger one reports it."""
         if format not in KV_FORMATS:
             raise SSAError(-2, f"format must be one of {sorted(KV_FORMATS)}")
         if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4:

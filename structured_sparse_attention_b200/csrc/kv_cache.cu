@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     const int exp = static_cast<int>(amax >> 23);
     const uint32_t man = amax & 0x7fffffu;
     const int E = FMT == SSA_KV_E4M3 ? exp - 8 + (man > 0x600000u) : exp - 2 + (man > 0x400000u);
-    return static_cast<uint32_t>(min(max(E, 16), FMT == SSA_KV_E4M3 ? 134 : 140));
+    return static_cast<uint32_t>(min(max(E, static_cast<int>(kScaleMin)), static_cast<int>(kv_scale_max(FMT))));
 }
 
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
@@ -432,6 +432,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 #pragma unroll
     for (int u = 0; u < kReadAhead; ++u) {
         if (!ok[u]) continue;
+        if constexpr (FMT != SSA_KV_BF16)
+            if (kv_bad_scale(FMT, E[u])) report(p.status, SSA_ERR_INVALID);
         uint4 v = raw[u];
         if constexpr (FMT == SSA_KV_E4M3) {
             const uint32_t f = kv_factor<FMT>(E[u]);

@@ -17,6 +17,11 @@ __host__ __device__ constexpr int kv_row_bytes(int fmt, int d) {
     return fmt == SSA_KV_BF16 ? 2 * d : fmt == SSA_KV_E4M3 ? d : d / 2;
 }
 
+// Scale bytes E that a cache holds, beside 255 (a group that is not finite).
+constexpr uint32_t kScaleMin = 16;
+__host__ __device__ constexpr uint32_t kv_scale_max(int fmt) { return fmt == SSA_KV_E4M3 ? 134 : 140; }
+__device__ __forceinline__ bool kv_bad_scale(int fmt, uint32_t E) { return E > kv_scale_max(fmt) && E != 255u; }
+
 // Checks shared by the entry points that take a cache.
 inline int check_cache(const char *fn, const ssa_kv_cache *c) {
     SSA_CHECK_ARG(c, "%s: null cache", fn);

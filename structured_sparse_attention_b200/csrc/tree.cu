@@ -339,14 +339,20 @@ struct Warp {
 
     // One step: the 16 keys of a ring step.
     __device__ __forceinline__ void step(const Rows &rows, const uint16_t *const *q_rows, const int *key,
-                                         const uint32_t *mask, uint32_t base, uint32_t scales, float scale_log2) {
+                                         const uint32_t *mask, uint32_t base, uint32_t scales, float scale_log2,
+                                         int32_t *status) {
         const int lane = threadIdx.x & 31, q = lane & 3, n = lane >> 2;
         uint32_t plain = 0xffffffffu;  // rows (keys, then values) whose scales are all exact in fp16
         if constexpr (kHalf) {
             uint32_t worst = 0;
 #pragma unroll
             for (int i = 0; i < D / SSA_KV_GROUP; ++i) worst = max(worst, ((scales >> (8 * i)) & 255u) - 113u);
-            plain = __ballot_sync(0xffffffffu, worst <= 29u);
+            plain = __ballot_sync(0xffffffffu, worst <= kv_scale_max(FMT) - 113u);
+            if (plain != 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < D / SSA_KV_GROUP; ++i)
+                    if (kv_bad_scale(FMT, (scales >> (8 * i)) & 255u)) report(status, SSA_ERR_INVALID);
+            }
         }
         float x[NT][4] = {};
         if ((plain & 0xffffu) != 0xffffu) {
@@ -586,7 +592,7 @@ struct Warp {
                 __syncwarp();  // all lanes' copies of this step are there, and the step to fill is free
                 if (more) issue(rows, key + (slot ^ 32) + i, ring + ahead, sc[2]);
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                step(rows, sh.q_rows, key + slot + i, mask + slot + i, ring + here, sc[0], p.scale_log2);
+                step(rows, sh.q_rows, key + slot + i, mask + slot + i, ring + here, sc[0], p.scale_log2, p.status);
                 sc[0] = sc[1];
                 sc[1] = sc[2];
                 here = here == 2 * R::kStep ? 0 : here + R::kStep;

@@ -103,8 +103,8 @@ struct Run {
 
 // Codes as fp16 pairs.  The hardware converts codes to fp16 (kv_cache.cuh's bf16 decoding takes
 // twice the instructions), and 2^(E - 127) keeps every code exact in fp16 for E in
-// [113, 142], which the append never exceeds and groups of zeros or with no value above
-// 448 * 2^-14 (e4m3) or 6 * 2^-14 (e2m1) leave; those go key by key in fp32.
+// [113, kv_scale_max], which groups of zeros or with no value above 448 * 2^-15 (e4m3) or 6 * 2^-15
+// (e2m1) leave; those go key by key in fp32.
 __device__ __forceinline__ uint32_t half_factors(uint32_t E0, uint32_t E1) {
     return ((E0 | (E1 << 16)) << 10) - 112u * 1024u * 0x10001u;
 }

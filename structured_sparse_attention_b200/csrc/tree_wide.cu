@@ -156,7 +156,7 @@ struct Quarter {
             for (int i = 0; i < kWords; ++i) c = bf2_fma(w[i], 0u, c);
             return (c & 0x7fff7fffu) == 0;
         } else {
-            return E - 113u <= 29u;
+            return E - 113u <= kv_scale_max(FMT) - 113u;
         }
     }
     __device__ __forceinline__ uint4 chunk(int j) const {
@@ -434,6 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
             bool odd = !(kr.plain(false) && vr.plain(true));
             odd = __shfl_xor_sync(0xffffffffu, odd, 1) || odd;
             odd = __shfl_xor_sync(0xffffffffu, odd, 2) || odd;
+            if constexpr (kHalf)
+                if (odd && (kv_bad_scale(FMT, kr.E) || kv_bad_scale(FMT, vr.E))) report(p.status, SSA_ERR_INVALID);
             uint8_t *tile = s_kv + 2 * st * C::kTile;
             kr.stage(tile, key, quarter, !odd);
             vr.stage(tile + C::kTile, key, quarter, !odd);

@@ -281,3 +281,24 @@ def test_captured_replayed_and_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(cache.v[0, :, 20:29], cache.v[0, :, 0:9])
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt,top", [("e4m3", 134), ("e2m1", 140)])
+def test_scale_bytes_out_of_range_are_reported(fmt, top, d):
+    m = ssa()
+    B, S = 2, 50
+    cache = m.KVCache(B, 3, S, d, fmt, device=dev())
+    ptr, row0 = t_i32([0, 30, 50]), t_i32([4, 7])
+    for t in (cache.k_scale, cache.v_scale):
+        for E in (0, 1, 16, 113, top, 255):
+            t[1, 2, 20, -1] = E
+            m.kv_read(cache, ptr, row0, 50)
+        for E in (top + 1, 142, 254):
+            t[1, 2, 20, -1] = E
+            with pytest.raises(m.SSAError) as e:
+                m.kv_read(cache, ptr, row0, 50)
+            assert e.value.code == -1
+        t[1, 2, 20, -1] = 127
+        t[1, 2, 40, -1] = top + 1  # a row that the call does not read
+        m.kv_read(cache, ptr, row0, 50)

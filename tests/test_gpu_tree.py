@@ -639,3 +639,29 @@ def test_first_calls_of_a_process_inside_a_capture():
     # what a launch asks of the device once (limits, clusters that fit) is asked while capturing
     out = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip().endswith("ok"), out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T", [2, 9, 33])
+@pytest.mark.parametrize("fmt,top", [("e4m3", 134), ("e2m1", 140)])
+def test_scale_bytes_out_of_range_are_reported(fmt, top, T):
+    # only of rows that the call reads; the other sequence's result is what it was
+    m = ssa()
+    S, d = 300, 128
+    D, C = [np.array([0, 3, 5], np.int32)] * 2, [np.array([11], np.int32)] * 2
+    cache, _ = make_cache(fmt, 2, 1, S, d, 1)
+    lists = m.tree_lists(m.extend(*lists_to_device(D, C)[0], S), 1, depth=1)
+    q = torch.randn(2, T, 2, d, device=dev()).bfloat16()
+    par, length = t_i32(np.full((2, T), -1, np.int32)), t_i32([150, 200])
+    call = lambda: m.attn_tree(q, cache, length, par, lists)
+    O, L = (x.clone() for x in call())
+    for t in (cache.k_scale, cache.v_scale):
+        keep = t.clone()
+        t[0, 0, 50] = top + 1  # nobody's
+        o, l = call()
+        assert torch.equal(o, O) and torch.equal(l, L)
+        for row, E in ((147, top + 1), (11, 142), (150, 254)):
+            t[0, 0, row, 2] = E
+            status = torch.zeros(1, dtype=torch.int32, device=dev())
+            o, l = m.attn_tree(q, cache, length, par, lists, status=status, check=False)
+            assert int(status) == -1 and torch.equal(o[1], O[1]) and torch.equal(l[1], L[1])
+            t.copy_(keep)
