@@ -13,7 +13,11 @@
 // fewer a 128-row tensor-memory tile would be mostly empty, and a step's time goes into
 // gathering and decoding the rows; fragments of mma.sync are filled from the gathered rows
 // as each warp has them, without a barrier between warps.  bf16 caches multiply as bf16, the
-// codes of e4m3 and e2m1 as fp16, which holds them exactly times their scale.
+// codes of e4m3 and e2m1 as fp16, which holds them exactly times their scale; steps with a group
+// too small for that multiply as bf16 too.  16 sequences x 8 KV heads over lists of 900 e4m3 keys,
+// 4 / 16 / 32 rows: 18.2 / 19.9 / 27.1 us, with values of deviation 0.005 20.5 / 21.5 / 30.2, with
+// such keys too 21.8 / 25.6 / 39.4 (key by key in fp32, as only values that are not finite go,
+// 104 / 184 / 344).
 //
 // Softmax: running maximum and sum per row in fp32, in the log2 domain.  On a bf16 cache a
 // weight p goes to the second product as bf16(p) + bf16(p - bf16(p)), 16 significant bits:
@@ -346,17 +350,12 @@ struct Warp {
         if constexpr (kHalf) {
             uint32_t worst = 0;
 #pragma unroll
-            for (int i = 0; i < D / SSA_KV_GROUP; ++i) worst = max(worst, ((scales >> (8 * i)) & 255u) - 113u);
-            plain = __ballot_sync(0xffffffffu, worst <= kv_scale_max(FMT) - 113u);
-            if (plain != 0xffffffffu) {
-#pragma unroll
-                for (int i = 0; i < D / SSA_KV_GROUP; ++i)
-                    if (kv_bad_scale(FMT, (scales >> (8 * i)) & 255u)) report(status, SSA_ERR_INVALID);
-            }
+            for (int i = 0; i < D / SSA_KV_GROUP; ++i) worst = max(worst, ((scales >> (8 * i)) & 255u) - kScaleHalf);
+            plain = __ballot_sync(0xffffffffu, worst <= kv_scale_max(FMT) - kScaleHalf);
         }
         float x[NT][4] = {};
         if ((plain & 0xffffu) != 0xffffu) {
-            logits_one_by_one(rows, q_rows, key, scale_log2, x);
+            logits_of_small_keys(q_rows, base, scales, scale_log2, x);
         } else {
             uint32_t kw[2][R::kKeyWords];
             R::load_key(base, n, q, kw[0]);
@@ -406,8 +405,20 @@ struct Warp {
         uint32_t vw[4][R::kValWords];
 #pragma unroll
         for (int t = 0; t < 4; ++t) R::load_val(base + 16 * R::kRow, 2 * q + (t & 1) + 8 * (t >> 1), n, vw[t]);
-        bool odd = (plain >> 16) != 0xffffu;
-        if constexpr (!kHalf) {
+        bool odd = false, small = false;  // values that are not finite; values for bf16
+        if constexpr (kHalf) {
+            if (plain != 0xffffffffu) {
+                bool big = false;
+#pragma unroll
+                for (int i = 0; i < D / SSA_KV_GROUP; ++i) {
+                    const uint32_t E = (scales >> (8 * i)) & 255u;
+                    big |= E > kv_scale_max(FMT);
+                    if (kv_bad_scale(FMT, E)) report(status, SSA_ERR_INVALID);
+                }
+                odd = (__ballot_sync(0xffffffffu, big) >> 16) != 0;
+                small = !odd && (plain >> 16) != 0xffffu;
+            }
+        } else {
             uint32_t c = 0;  // x * 0 is NaN for an infinity or a NaN, and stays one
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -417,6 +428,8 @@ struct Warp {
         }
         if (odd) {
             one_by_one(rows, key, mask, x);
+        } else if (!kHalf || small) {
+            products_bf16(base, scales, vw, x);
         } else if constexpr (kHalf) {
             // weights as fp16: 2^-12 of the weight, or 2^-25 where it is below 2^-14 (the largest
             // is 1 or more): against the output's 2^-9 one product is enough
@@ -465,52 +478,114 @@ struct Warp {
                     }
                 }
             }
-        } else {
-            uint32_t hi[NT][2], lo[NT][2];
+        }
+    }
+
+    // The scale bytes of a row from lane `src`, and the factor of its group `g`.
+    static __device__ __forceinline__ uint32_t row_factor(uint32_t scales, int src, int g) {
+        return kv_factor<FMT>((__shfl_sync(0xffffffffu, scales, src) >> (8 * g)) & 255u);
+    }
+
+    // Logits where a scale is below fp16's exact range: the step's keys as bf16, with Q's rows as
+    // they are.
+    __device__ __forceinline__ void logits_of_small_keys(const uint16_t *const *q_rows, uint32_t base, uint32_t scales,
+                                                         float scale_log2, float (&x)[NT][4]) const {
+        if constexpr (kHalf) {
+            const int lane = threadIdx.x & 31, q = lane & 3, n = lane >> 2;
+            uint32_t f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) f[k] = row_factor(scales, n + 8 * k, q * (D / 4) / SSA_KV_GROUP);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                uint32_t kw[2][R::kKeyWords];
+                R::load_key(base, n, q, kw[0]);
+                R::load_key(base, n + 8, q, kw[1]);
+                const uint16_t *const src[1] = {q_rows[8 * t + n]};
+                uint32_t w[1][D / 8];
+                Warp<D, FMT, 1>::fetch_q(src, w);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float a = x[t][2 * k], b = x[t][2 * k + 1];
-                    const uint32_t w = pack_bf16(a, b);
-                    hi[t][k] = transpose8x8(w);
-                    lo[t][k] =
-                        transpose8x8(pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)));
+                for (int s = 0; s < D / 16; ++s) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t u, v;
+                        if constexpr (FMT == SSA_KV_E4M3) {
+                            decode_e4m3(kw[k][s], f[k], u, v);
+                            a[k] = prmt(u, v, 0x5410u);
+                            a[2 + k] = prmt(u, v, 0x7632u);
+                        } else {
+                            decode_e2m1(kw[k][s / 2] >> (16 * (s & 1)), f[k], a[k], a[2 + k]);
+                        }
+                    }
+                    mma_bf16(x[t], a, w[0][2 * s], w[0][2 * s + 1]);
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                const uint32_t a[4] = {prmt(vw[0][j], vw[1][j], 0x5410u), prmt(vw[0][j], vw[1][j], 0x7632u),
-                                       prmt(vw[2][j], vw[3][j], 0x5410u), prmt(vw[2][j], vw[3][j], 0x7632u)};
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma_bf16(o[t][j], a, hi[t][0], hi[t][1]);
-                    mma_bf16(o[t][j], a, lo[t][0], lo[t][1]);
-                }
+                for (int c = 0; c < 4; ++c) x[t][c] *= scale_log2 / scale[t][c & 1];  // in the units of the row's products
             }
         }
     }
 
-    // Logits where a scale is outside fp16's exact range: fp32, from the stored rows and Q.
-    __device__ __forceinline__ void logits_one_by_one(const Rows &rows, const uint16_t *const *q_rows, const int *key,
-                                                      float scale_log2, float (&x)[NT][4]) const {
-        const int lane = threadIdx.x & 31, q = lane & 3, n = lane >> 2;
+    // O += V^T P^T over bf16 values, those of a bf16 cache or decoded, with P in two parts.
+    __device__ __forceinline__ void products_bf16(uint32_t base, uint32_t scales, const uint32_t (&vw)[4][R::kValWords],
+                                                  const float (&x)[NT][4]) {
+        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint16_t *qr = q_rows[8 * t + 2 * q + (c & 1)];
-                const int j = key[n + 8 * (c >> 1)];
-                float sum = 0.0f;
-#pragma unroll 1
-                for (int i = 0; qr && i < D / 8; ++i) {
-                    Run<FMT, 8> run;
-                    run.load(rows.k, rows.ks, j, D, i);
+            for (int k = 0; k < 2; ++k) {
+                const float a = x[t][2 * k], b = x[t][2 * k + 1];
+                const uint32_t w = pack_bf16(a, b);
+                hi[t][k] = transpose8x8(w);
+                lo[t][k] = transpose8x8(pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)));
+            }
+        }
+        const auto product = [&](int j, const uint32_t(&a)[4]) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum = fmaf(__uint_as_float(static_cast<uint32_t>(__ldg(qr + 8 * i + e)) << 16), run.value(e), sum);
+            for (int t = 0; t < NT; ++t) {
+                mma_bf16(o[t][j], a, hi[t][0], hi[t][1]);
+                mma_bf16(o[t][j], a, lo[t][0], lo[t][1]);
+            }
+        };
+        if constexpr (!kHalf) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                const uint32_t a[4] = {prmt(vw[0][j], vw[1][j], 0x5410u), prmt(vw[0][j], vw[1][j], 0x7632u),
+                                       prmt(vw[2][j], vw[3][j], 0x5410u), prmt(vw[2][j], vw[3][j], 0x7632u)};
+                product(j, a);
+            }
+        } else {
+            const int lane = threadIdx.x & 31, q = lane & 3, n = lane >> 2;
+            uint32_t f[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                f[t] = row_factor(scales, 16 + 2 * q + (t & 1) + 8 * (t >> 1), n * (D / 8) / SSA_KV_GROUP);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {  // four elements of each key
+                uint32_t u[4], v[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {  // read again: held since the fast path's load, the words would be spilled
+                    uint32_t w;
+                    lds_words<1>(R::word(base + 16 * R::kRow, 2 * q + (t & 1) + 8 * (t >> 1),
+                                         4 * (n * R::kValWords + (FMT == SSA_KV_E4M3 ? i : i / 2))),
+                                 &w);
+                    if constexpr (FMT == SSA_KV_E4M3) decode_e4m3(w, f[t], u[t], v[t]);
+                    else decode_e2m1(w >> (16 * (i & 1)), f[t], u[t], v[t]);
                 }
-                x[t][c] = sum * (scale_log2 / scale[t][c & 1]);  // in the units of the row's products
+                if constexpr (FMT == SSA_KV_E4M3) {  // u: elements 0 and 2, v: 1 and 3
+                    const uint32_t a[4] = {prmt(u[0], u[1], 0x5410u), prmt(v[0], v[1], 0x5410u), prmt(u[2], u[3], 0x5410u),
+                                           prmt(v[2], v[3], 0x5410u)};
+                    const uint32_t b[4] = {prmt(u[0], u[1], 0x7632u), prmt(v[0], v[1], 0x7632u), prmt(u[2], u[3], 0x7632u),
+                                           prmt(v[2], v[3], 0x7632u)};
+                    product(2 * i, a);
+                    product(2 * i + 1, b);
+                } else {  // u: elements 0 and 1, v: 2 and 3
+                    const uint32_t a[4] = {prmt(u[0], u[1], 0x5410u), prmt(u[0], u[1], 0x7632u), prmt(u[2], u[3], 0x5410u),
+                                           prmt(u[2], u[3], 0x7632u)};
+                    const uint32_t b[4] = {prmt(v[0], v[1], 0x5410u), prmt(v[0], v[1], 0x7632u), prmt(v[2], v[3], 0x5410u),
+                                           prmt(v[2], v[3], 0x7632u)};
+                    product(2 * i, a);
+                    product(2 * i + 1, b);
+                }
             }
         }
     }
