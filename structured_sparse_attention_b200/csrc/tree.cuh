@@ -104,8 +104,8 @@ struct Run {
 // Codes as fp16 pairs.  The hardware converts codes to fp16 (kv_cache.cuh's bf16 decoding takes
 // twice the instructions), and 2^(E - 127) keeps every code exact in fp16 for E in
 // [113, kv_scale_max].  Groups of zeros or with no value above 448 * 2^-15 (e4m3) or 6 * 2^-15
-// (e2m1) lie below; a step or tile that has one is decoded to bf16, exact for every scale, and
-// multiplied as a bf16 cache's.
+// (e2m1) lie below; they are decoded to bf16, exact for every scale, and multiplied as a bf16
+// cache's: the step that has one, or the list of a CTA with tensor-memory tiles.
 constexpr uint32_t kScaleHalf = 113;  // the smallest scale byte of the fp16 products
 __device__ __forceinline__ uint32_t half_factors(uint32_t E0, uint32_t E1) {
     return ((E0 | (E1 << 16)) << 10) - 112u * 1024u * 0x10001u;

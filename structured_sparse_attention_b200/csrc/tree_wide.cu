@@ -20,9 +20,13 @@
 // waiter, so a parity stands for one phase only.
 //
 // Quantised caches become fp16 tiles (every code is exact while the scale is in fp16's
-// range) and P is fp16; bf16 caches stay bf16 and P is split into two bf16 (see tree.cu).
-// A key whose scales are outside that range, or with a value that is not finite, is taken
-// out of the tile (zeros, no row bits) and added in fp32 by the rows that retain it.
+// range) and P is fp16; bf16 caches stay bf16 and P is split into two bf16 (see tree.cu).  A
+// CTA that meets a group below that range (but for zeros) gives its pass up and takes its list
+// again with bf16 tiles, in code out of line: 16 trees of 64 nodes over 1000 e4m3 keys 62 us, 103 with
+// values of deviation 0.005, at most about 130 where the only small group is the last (key by key such
+// values took 14.7 ms).  Both kinds of tile in one loop cost the usual ones 15 %, bf16 tiles for
+// all 11 % (37 % on lists of 7400 keys).  A key with a value that is not finite is taken out of
+// the tile (zeros, no row bits) and added in fp32 by the rows that retain it.
 //
 // One CTA of 16 warps an SM, each role in warps of its own: with resolving, decoding and
 // issuing in one group of four warps and two CTAs an SM, every step of the chain waited for
@@ -68,11 +72,16 @@ struct Wide {
     static constexpr int kBytes = (kBig > kMin ? kBig : kMin) + 1024;  // + alignment
 };
 
-struct WideShared : TreeInfo {
+struct Barriers {
     uint64_t resolved[kEntries], turned[kEntries], entry_free[kEntries];
     uint64_t full[kRing], s_full[kRing], p_full[kRing], pv_done[kRing], drain;
+};
+
+struct WideShared : TreeInfo {
+    Barriers bars[2];  // of the first and of a second pass
     uint32_t tmem;
     int abort;
+    int small;  // the pass met a group below fp16's exact range
     // ring of resolved tiles; mask: bit i of word w = row first + 32 w + i retains the key
     int key[kEntries][kN];
     uint32_t mask[kEntries][4][kN];
@@ -148,24 +157,49 @@ struct Quarter {
         if constexpr (FMT != SSA_KV_BF16)
             E = __ldg(scales + static_cast<uint64_t>(row) * (D / SSA_KV_GROUP) + quarter * (D / 4) / SSA_KV_GROUP);
     }
-    __device__ __forceinline__ bool plain(bool value) const {
+    // not finite: the key is taken out of its tile
+    __device__ __forceinline__ bool odd(bool value) const {
         if constexpr (FMT == SSA_KV_BF16) {
-            if (!value) return true;  // a key's infinities and NaN stay in its own logits
-            uint32_t c = 0;           // x * 0 is NaN for an infinity or a NaN, and stays one
+            if (!value) return false;  // a key's infinities and NaN stay in its own logits
+            uint32_t c = 0;            // x * 0 is NaN for an infinity or a NaN, and stays one
 #pragma unroll
             for (int i = 0; i < kWords; ++i) c = bf2_fma(w[i], 0u, c);
-            return (c & 0x7fff7fffu) == 0;
+            return (c & 0x7fff7fffu) != 0;
         } else {
-            return E - 113u <= kv_scale_max(FMT) - 113u;
+            return E > kv_scale_max(FMT);
         }
     }
+    // below fp16's exact range, and not all zero
+    __device__ __forceinline__ bool small() const {
+        if (FMT == SSA_KV_BF16 || E >= kScaleHalf) return false;
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) c |= w[i];
+        return (c & (FMT == SSA_KV_E4M3 ? 0x7f7f7f7fu : 0x77777777u)) != 0;
+    }
+
+    template <bool HALF>
     __device__ __forceinline__ uint4 chunk(int j) const {
         uint32_t d[4];
         if constexpr (FMT == SSA_KV_BF16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = w[4 * j + i];
+        } else if constexpr (!HALF) {
+            const uint32_t f = kv_factor<FMT>(E);
+            if constexpr (FMT == SSA_KV_E4M3) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t even, odd;
+                    decode_e4m3(w[2 * j + i], f, even, odd);
+                    d[2 * i] = prmt(even, odd, 0x5410u);
+                    d[2 * i + 1] = prmt(even, odd, 0x7632u);
+                }
+            } else {
+                decode_e2m1(w[j], f, d[0], d[1]);
+                decode_e2m1(w[j] >> 16, f, d[2], d[3]);
+            }
         } else {
-            const uint32_t f = half_factors(E, E);
+            const uint32_t e = max(E, kScaleHalf), f = half_factors(e, e);  // a lower E has codes of zero
             if constexpr (FMT == SSA_KV_E4M3) {
                 d[0] = half_e4m3(w[2 * j]);
                 d[1] = half_e4m3(w[2 * j] >> 16);
@@ -180,24 +214,25 @@ struct Quarter {
         return make_uint4(d[0], d[1], d[2], d[3]);
     }
     // to the row of a tile; zeros where the key is taken out
+    template <bool HALF>
     __device__ __forceinline__ void stage(uint8_t *tile, int key, int quarter, bool keep) const {
         constexpr int kChunks = D / 32;  // of this quarter
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
             const int c = (quarter * kChunks + j) & 7, panel = (quarter * kChunks + j) >> 3;
-            const uint4 v = keep ? chunk(j) : make_uint4(0, 0, 0, 0);
+            const uint4 v = keep ? chunk<HALF>(j) : make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4 *>(tile + panel * (kN * 128) + key * 128 + ((c ^ (key & 7)) << 4)) = v;
         }
     }
 };
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __grid_constant__ TreeParams p) {
+// The work of a CTA, with fp16 tiles (HALF) or bf16 ones.  False, with no output and the tensor memory
+// still held, if a pass with fp16 tiles met a group below their exact range.
+template <int D, int FMT, bool HALF>
+__device__ __forceinline__ bool attend(const TreeParams &p, WideShared &sh, uint8_t *smem) {
     using C = Wide<D>;
-    constexpr bool kHalf = FMT != SSA_KV_BF16;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ WideShared sh;
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr bool kFirst = HALF || FMT == SSA_KV_BF16;  // else after such a pass
+    Barriers &bars = sh.bars[kFirst ? 0 : 1];
     uint8_t *const s_q = smem, *const s_kv = smem + C::kQ;  // stage s: K at 2 s kTile, V behind it
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int slice = blockIdx.x % p.slices, first = (blockIdx.x / p.slices) * kM;
@@ -211,29 +246,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
     nn = min(max(nn, 0), p.T);
     if (first >= G * nn) {  // every CTA of the cluster alike
         if (bad && g == 0 && first == 0 && slice == 0 && tid == 0) report(p.status, SSA_ERR_INVALID);
-        return;
+        return true;
     }
     const int last = min(first + kM, G * nn);
     if (tid == 0) {
         sh.bad = bad;
         sh.max_depth = 0;
-        sh.abort = 0;
+        sh.abort = sh.small = 0;
         set_problem(p, sh.w, g, len, nn, first, last, hp, G);
         uint32_t here = 0;
         for (int hh = first / nn; hh < 16 && hh * nn < last; ++hh) here |= 1u << hh;
         sh.here = here;
         for (int s = 0; s < kEntries; ++s) {
-            mbar_init(&sh.resolved[s], kResolvers);
-            mbar_init(&sh.turned[s], 32);
-            mbar_init(&sh.entry_free[s], 1);
+            mbar_init(&bars.resolved[s], kResolvers);
+            mbar_init(&bars.turned[s], 32);
+            mbar_init(&bars.entry_free[s], 1);
         }
         for (int s = 0; s < kRing; ++s) {
-            mbar_init(&sh.full[s], kProducers);
-            mbar_init(&sh.s_full[s], 1);
-            mbar_init(&sh.p_full[s], kM);
-            mbar_init(&sh.pv_done[s], 1);
+            mbar_init(&bars.full[s], kProducers);
+            mbar_init(&bars.s_full[s], 1);
+            mbar_init(&bars.p_full[s], kM);
+            mbar_init(&bars.pv_done[s], 1);
         }
-        mbar_init(&sh.drain, 1);
+        mbar_init(&bars.drain, 1);
         fence_barrier_init();
     } else if (tid == 32) {
         set_lengths(p, sh.w, g, len, bad);
@@ -251,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
         sh.spread[set][tid & 15] = make_uint4(rows[0], rows[1], rows[2], rows[3]);
     }
     if (tid >= 128 && tid < 144) set_heads(p, sh.w, hp, G, tid - 128);
-    if (warp == kWarpMma) {
+    if (kFirst && warp == kWarpMma) {
         tmem_alloc(&sh.tmem, kTmemCols);
         tmem_relinquish();
     }
@@ -286,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
     // Q's rows into shared memory, O to zero
     float scale = p.scale_log2, shift = 1.0f;
     if (tid < kM) {
-        if (kHalf) {
+        if (HALF) {
             uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
@@ -303,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
         }
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-            if (kHalf) {
+            if (HALF) {
                 uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -332,7 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
     const int total = bad ? 0 : w.n_off + w.n_col + nn;
     const int tiles_all = (total + kN - 1) / kN;
     const int tiles = tiles_all > slice ? (tiles_all - slice + p.slices - 1) / p.slices : 0;  // slice, slice + slices, ..
-    volatile int *abort = &sh.abort;
+    volatile int *abort = &sh.abort, *small = &sh.small;
+    const auto give_up = [&] {  // after a wait that ended without its phase
+        if (!HALF || !*small) report(p.status, SSA_ERR_TIMEOUT);
+        *abort = 1;
+    };
     const int64_t lim = p.wait_ns;
     float m = -3.402823466e38f, l = 0.0f;  // this row's reference (log2 domain) and sum
 
@@ -341,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
             const int slot = i % kEntries;
-            if (!__all_sync(0xffffffffu, wait_asleep(&sh.resolved[slot], (i / kEntries) & 1, lim, abort))) {
+            if (!__all_sync(0xffffffffu, wait_asleep(&bars.resolved[slot], (i / kEntries) & 1, lim, abort))) {
                 ok = false;
                 break;
             }
@@ -351,12 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                 sh.keys[slot][0][32 * q + lane] = transpose32(sh.mask[slot][q][lane]);
                 sh.keys[slot][1][32 * q + lane] = transpose32(sh.mask[slot][q][32 + lane]);
             }
-            mbar_arrive(&sh.turned[slot]);
+            mbar_arrive(&bars.turned[slot]);
         }
-        if (!ok) {
-            report(p.status, SSA_ERR_TIMEOUT);
-            *abort = 1;
-        }
+        if (!ok) give_up();
     } else if (warp >= kWarpResolve && warp < kWarpMma) {
         // ------------------------------ resolvers ------------------------------
         const int e = tid - 32 * kWarpResolve;
@@ -394,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
             peek(now);
             const int slot = i % kEntries;
             if (i >= kEntries &&
-                !__all_sync(0xffffffffu, wait_asleep(&sh.entry_free[slot], ((i - kEntries) / kEntries) & 1, lim, abort))) {
+                !__all_sync(0xffffffffu, wait_asleep(&bars.entry_free[slot], ((i - kEntries) / kEntries) & 1, lim, abort))) {
                 ok = false;
                 break;
             }
@@ -402,19 +438,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
             sh.key[slot][e] = (v.v[0] | v.v[1] | v.v[2] | v.v[3]) ? j_now : w.len;
 #pragma unroll
             for (int k = 0; k < 4; ++k) sh.mask[slot][k][e] = v.v[k];
-            mbar_arrive(&sh.resolved[slot]);
+            mbar_arrive(&bars.resolved[slot]);
         }
-        if (!ok) {
-            report(p.status, SSA_ERR_TIMEOUT);
-            *abort = 1;
-        }
+        if (!ok) give_up();
     } else if (warp >= kWarpProduce && warp < kWarpResolve) {
         // ------------------------------ producers ------------------------------
         const int pt = tid - 32 * kWarpProduce, key = pt >> 2, quarter = pt & 3;
         Quarter<D, FMT> kr, vr, kn, vn;
         bool ok = true;
         const auto load = [&](int i) {  // rows of tile i, once it is resolved
-            ok = __all_sync(0xffffffffu, wait_asleep(&sh.resolved[i % kEntries], (i / kEntries) & 1, lim, abort));
+            ok = __all_sync(0xffffffffu, wait_asleep(&bars.resolved[i % kEntries], (i / kEntries) & 1, lim, abort));
             if (!ok) return;
             const int j = sh.key[i % kEntries][key];
             kn.load(rows.k, rows.ks, j, quarter);
@@ -427,36 +460,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
             vr = vn;
             if (i + 1 < tiles) load(i + 1);
             if (!ok) break;
-            if (i >= kRing && !__all_sync(0xffffffffu, wait_asleep(&sh.pv_done[st], ((i - kRing) / kRing) & 1, lim, abort))) {
+            if (i >= kRing && !__all_sync(0xffffffffu, wait_asleep(&bars.pv_done[st], ((i - kRing) / kRing) & 1, lim, abort))) {
                 ok = false;
                 break;
             }
-            bool odd = !(kr.plain(false) && vr.plain(true));
+            if constexpr (HALF) {
+                if (__any_sync(0xffffffffu, kr.small() || vr.small())) {  // the pass ends
+                    *small = 1;
+                    ok = false;
+                    break;
+                }
+            }
+            bool odd = kr.odd(false) || vr.odd(true);
             odd = __shfl_xor_sync(0xffffffffu, odd, 1) || odd;
             odd = __shfl_xor_sync(0xffffffffu, odd, 2) || odd;
-            if constexpr (kHalf)
+            if constexpr (FMT != SSA_KV_BF16)
                 if (odd && (kv_bad_scale(FMT, kr.E) || kv_bad_scale(FMT, vr.E))) report(p.status, SSA_ERR_INVALID);
             uint8_t *tile = s_kv + 2 * st * C::kTile;
-            kr.stage(tile, key, quarter, !odd);
-            vr.stage(tile + C::kTile, key, quarter, !odd);
+            kr.template stage<HALF>(tile, key, quarter, !odd);
+            vr.template stage<HALF>(tile + C::kTile, key, quarter, !odd);
             if (quarter == 0) sh.odd[st][key] = odd;
             fence_async_shared();
-            mbar_arrive(&sh.full[st]);
+            mbar_arrive(&bars.full[st]);
         }
-        if (!ok) {
-            report(p.status, SSA_ERR_TIMEOUT);
-            *abort = 1;
-        }
+        if (!ok) give_up();
     } else if (warp == kWarpMma) {
         // ------------------------------ MMA issuer ------------------------------
         if (lane == 0) {
-            constexpr uint32_t kQK = instr_desc(!kHalf, kN, false), kPV = instr_desc(!kHalf, D, true);
+            constexpr uint32_t kQK = instr_desc(!HALF, kN, false), kPV = instr_desc(!HALF, D, true);
             const uint32_t aq = smem_u32(s_q), akv = smem_u32(s_kv);
             bool ok = true;
             for (int i = 0; i <= tiles; ++i) {
                 if (i < tiles) {
                     const int st = i % kRing;
-                    if (!mbar_wait_poll(&sh.full[st], (i / kRing) & 1, lim, abort)) {
+                    if (!mbar_wait_poll(&bars.full[st], (i / kRing) & 1, lim, abort)) {
                         ok = false;
                         break;
                     }
@@ -466,11 +503,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                     for (int k = 0; k < D / 16; ++k)
                         umma_ss(tmem + kN * st, smem_desc(aq + (k >> 2) * (kM * 128) + (k & 3) * 32, 16, 1024),
                                 smem_desc(ak + (k >> 2) * (kN * 128) + (k & 3) * 32, 16, 1024), kQK, k > 0 ? 1u : 0u);
-                    umma_commit(&sh.s_full[st]);
+                    umma_commit(&bars.s_full[st]);
                 }
                 if (i > 0) {
                     const int st = (i - 1) % kRing;
-                    if (!mbar_wait_poll(&sh.p_full[st], ((i - 1) / kRing) & 1, lim, abort)) {
+                    if (!mbar_wait_poll(&bars.p_full[st], ((i - 1) / kRing) & 1, lim, abort)) {
                         ok = false;
                         break;
                     }
@@ -480,18 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                     for (int k = 0; k < kN / 16; ++k) {  // 16 keys: 16 rows of 128 bytes
                         const uint64_t dv = smem_desc(av + k * 2048, kN * 128, 1024);
                         umma_ts(tmem + kColO, tmem + kN * st + 8 * k, dv, kPV, 1u);
-                        if (!kHalf) umma_ts(tmem + kColO, tmem + kN * st + 32 + 8 * k, dv, kPV, 1u);
+                        if (!HALF) umma_ts(tmem + kColO, tmem + kN * st + 32 + 8 * k, dv, kPV, 1u);
                     }
-                    umma_commit(&sh.pv_done[st]);
-                    umma_commit(&sh.entry_free[(i - 1) % kEntries]);
+                    umma_commit(&bars.pv_done[st]);
+                    umma_commit(&bars.entry_free[(i - 1) % kEntries]);
                 }
             }
-            if (!ok) {
-                report(p.status, SSA_ERR_TIMEOUT);
-                *abort = 1;
-            }
-            umma_commit(&sh.drain);  // completes once every MMA issued is done
-            mbar_wait(&sh.drain, 0, kDrainNs, nullptr);
+            if (!ok) give_up();
+            umma_commit(&bars.drain);  // completes once every MMA issued is done
+            mbar_wait(&bars.drain, 0, kDrainNs, nullptr);
         }
         __syncwarp();
     } else {
@@ -509,12 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
             const int parity = (i / kRing) & 1, slot = i % kEntries;
             // (P V of tile i - kRing is done by then; observed here so that no wait on pv_done is ever
             // more than one phase behind)
-            const bool there = mbar_test(&sh.full[st], parity) & mbar_test(&sh.s_full[st], parity) &
-                               mbar_test(&sh.turned[slot], (i / kEntries) & 1) &
-                               (i < kRing || mbar_test(&sh.pv_done[st], parity ^ 1));
+            const bool there = mbar_test(&bars.full[st], parity) & mbar_test(&bars.s_full[st], parity) &
+                               mbar_test(&bars.turned[slot], (i / kEntries) & 1) &
+                               (i < kRing || mbar_test(&bars.pv_done[st], parity ^ 1));
             if (!__all_sync(0xffffffffu, there) &&
-                (!wait(&sh.full[st], parity) || !wait(&sh.s_full[st], parity) ||
-                 !wait(&sh.turned[slot], (i / kEntries) & 1) || (i >= kRing && !wait(&sh.pv_done[st], parity ^ 1))))
+                (!wait(&bars.full[st], parity) || !wait(&bars.s_full[st], parity) ||
+                 !wait(&bars.turned[slot], (i / kEntries) & 1) || (i >= kRing && !wait(&bars.pv_done[st], parity ^ 1))))
                 break;
             tc_fence_after();
             if (any_row) {
@@ -524,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                 const bool some_special = (special[0] | special[1]) != 0;
                 if (some_special) {
                     if (i > 0) {
-                        if (!wait(&sh.pv_done[before], ((i - 1) / kRing) & 1)) break;
+                        if (!wait(&bars.pv_done[before], ((i - 1) / kRing) & 1)) break;
                         tc_fence_after();
                     }
 #pragma unroll 1
@@ -586,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                     l *= f;
                     if (i > 0 || some_special) {  // else O is still zero
                         if (i > 0 && !some_special) {
-                            if (!wait(&sh.pv_done[before], ((i - 1) / kRing) & 1)) break;
+                            if (!wait(&bars.pv_done[before], ((i - 1) / kRing) & 1)) break;
                             tc_fence_after();
                         }
 #pragma unroll 1
@@ -627,10 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     const float x = __uint_as_float(r[2 * k]), y = __uint_as_float(r[2 * k + 1]);
-                    hi[k] = kHalf ? pack_half(x, y) : pack_bf16(x, y);
+                    hi[k] = HALF ? pack_half(x, y) : pack_bf16(x, y);
                 }
                 tmem_st32(t_s, hi);
-                if constexpr (!kHalf) {
+                if constexpr (!HALF) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         hi[k] = pack_bf16(__uint_as_float(r[2 * k]) - __uint_as_float(hi[k] << 16),
@@ -640,18 +674,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
                 tmem_wait_st();
                 tc_fence_before();
             }
-            mbar_arrive(&sh.p_full[st]);
+            mbar_arrive(&bars.p_full[st]);
         }
         // the last tile's P V
-        if (ok && tiles > 0 && wait(&sh.pv_done[(tiles - 1) % kRing], ((tiles - 1) / kRing) & 1)) tc_fence_after();
-        if (!ok) {
-            report(p.status, SSA_ERR_TIMEOUT);
-            *abort = 1;
-        }
+        if (ok && tiles > 0 && wait(&bars.pv_done[(tiles - 1) % kRing], ((tiles - 1) / kRing) & 1)) tc_fence_after();
+        if (!ok) give_up();
     }
     // Every MMA is done (the issuer has waited for its own), Q and the tiles are no longer read.
     tc_fence_before();
     __syncthreads();
+    if (HALF && *small) return false;
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
     if (warp < 4 && first + 32 * warp < last) {
@@ -699,11 +731,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __gri
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    if (p.slices == 1) return;
+    if (p.slices == 1) return true;
     join_parts<D, 1>(
         p, w, b, slice, warp, kThreads / 32, [&](int, int i) { return sh.ml[i]; },
         [&](int, int i) { return part + i * C::kPartPitch; });
     cluster.sync();  // a part stays until the cluster has read it
+    return true;
+}
+
+// The pass with bf16 tiles after one with fp16 tiles that met a small group.
+template <int D, int FMT>
+__device__ __noinline__ void attend_small(const TreeParams &p, WideShared &sh, uint8_t *smem) {
+    __syncthreads();  // all threads have left the first pass
+    attend<D, FMT, false>(p, sh, smem);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel(const __grid_constant__ TreeParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ WideShared sh;
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr bool kHalf = FMT != SSA_KV_BF16;
+    if (!attend<D, FMT, kHalf>(p, sh, smem) && kHalf) attend_small<D, FMT>(p, sh, smem);
 }
 
 template <int D, int FMT>

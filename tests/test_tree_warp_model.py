@@ -117,8 +117,7 @@ def test_tensor_memory_is_read_by_whole_warps():
     # attn_tree_wide_kernel: code that runs in some lanes of a warp (a loop under a lane's own
     # condition, stores of the rows that exist) is followed by a warp barrier before the next
     # access to tensor memory, which is an instruction of the whole warp
-    src = source("tree_wide.cu")
-    kernel = src[src.index("void __launch_bounds__(kThreads, 1) attn_tree_wide_kernel"):]
+    kernel = source("tree_wide.cu")
     loop = kernel.index("in && c < D / 8")
     assert "__syncwarp();" in kernel[loop:kernel.index("tmem_ld8(", loop)]
     last = kernel.index("const bool direct")
