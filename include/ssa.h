@@ -579,7 +579,7 @@ SSA_API int sparse_tree_lists(const ssa_plan *plan, int H_kv, int depth, const i
  * so that a node's result is the row that sparse_attn_decode gives once its path is
  * committed; one node per sequence is the ordinary decoding step, over a cache of any
  * format.  No key: O = 0, LSE = -inf.  A logit of -inf has no weight.  fp32 logits and
- * statistics, weights of 11 bits of the largest one at least, bf16 O; values in rows that a query
+ * statistics; weights of 11 bits at least, or to 2^-32 of a row's largest; bf16 O.  Values in rows that a query
  * does not retain do not touch it, NaN and infinities included.
  *
  *   Q, O      device bf16 [B][T][H_q][d], contiguous, 16-byte aligned (not the same buffer)

@@ -112,8 +112,8 @@ __device__ __forceinline__ void resolve(const Entry &x, const TreeParams &p, con
 // consecutive outputs of the rows 2q and 2q + 1 of each block, and its logits are of the
 // same rows, so rescaling O needs no exchange either.
 //
-// The reference of the softmax moves only when a logit exceeds it by 2^8 (weights then stay
-// below 256, sums in fp32): one vote a step instead of a maximum over the warp.
+// The reference of the softmax moves only when a logit exceeds it by 2^8, less kLift (weights
+// then stay below 2^15, sums in fp32): one vote a step instead of a maximum over the warp.
 //
 // Rows travel by cp.async into a ring of three steps of the warp's own, two steps ahead of
 // their use: 2 x 4 KB a warp in flight (e4m3, d = 128) without a register, no CTA barrier.
@@ -194,8 +194,6 @@ struct Warp {
     using R = Ring<D, FMT>;
     using VRun = Run<FMT, D / 8>;
     static constexpr bool kHalf = FMT != SSA_KV_BF16;
-    static constexpr float kSlack = 8.0f;
-
     static constexpr bool kQueryShared = NT > 2;  // O takes the registers; the CTA's fragments lie in shared memory
     static constexpr int kQueryBytes = kQueryShared ? NT * (D / 16) * 32 * 8 : 0;
 
@@ -304,7 +302,7 @@ struct Warp {
                 const bool in = (((c & 2) ? mask1 : mask0) >> (8 * t + 2 * q + (c & 1))) & 1;
                 if (!in) x[t][c] = -INFINITY;
                 y[t][c] = fmaf(x[t][c], scale[t][c & 1], -m[t][c & 1]);
-                over |= y[t][c] > kSlack;
+                over |= y[t][c] > kSlack + kLift<kHalf>;
             }
         }
         if (__any_sync(0xffffffffu, over)) {
@@ -312,7 +310,7 @@ struct Warp {
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float top = fmaxf(m[t][k], fmaxf(x[t][k], x[t][2 + k]) * scale[t][k]);
+                    float top = fmaxf(m[t][k], fmaf(fmaxf(x[t][k], x[t][2 + k]), scale[t][k], -kLift<kHalf>));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                     const float f = ex2_approx(m[t][k] - top);
@@ -432,7 +430,7 @@ struct Warp {
             products_bf16(base, scales, vw, x);
         } else if constexpr (kHalf) {
             // weights as fp16: 2^-12 of the weight, or 2^-25 where it is below 2^-14 (the largest
-            // is 1 or more): against the output's 2^-9 one product is enough
+            // is 2^7 or more): against the output's 2^-9 one product is enough
             uint32_t w[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {

@@ -101,6 +101,12 @@ struct Run {
     }
 };
 
+// Weights that become fp16 are kept 2^kLift times as large: at most 2^(kSlack + kLift) = 2^15, and what
+// falls below fp16's range is 2^-32 of the largest weight.
+constexpr float kSlack = 8.0f;  // a reference moves when a logit (log2 domain) exceeds it by more
+template <bool HALF>
+constexpr float kLift = HALF ? 7.0f : 0.0f;
+
 // Codes as fp16 pairs.  The hardware converts codes to fp16 (kv_cache.cuh's bf16 decoding takes
 // twice the instructions), and 2^(E - 127) keeps every code exact in fp16 for E in
 // [113, kv_scale_max].  Groups of zeros or with no value above 448 * 2^-15 (e4m3) or 6 * 2^-15

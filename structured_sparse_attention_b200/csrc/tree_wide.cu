@@ -55,7 +55,6 @@ constexpr int kWarpProduce = 4, kWarpResolve = 12, kWarpMma = 14, kWarpTurn = 15
 constexpr uint32_t kTmemCols = 512;      // S, P: kRing x 64, O: d
 constexpr uint32_t kColO = kRing * kN;
 constexpr int64_t kDrainNs = 1000000000LL;
-constexpr float kSlack = 8.0f;
 
 template <int D>
 struct Wide {
@@ -577,7 +576,7 @@ __device__ __forceinline__ bool attend(const TreeParams &p, WideShared &sh, uint
                         }
                         __syncwarp();  // the loop ran in some lanes; tensor memory is read by the whole warp
                         const float y = in ? dot * p.scale_log2 : -INFINITY;
-                        const float up = fmaxf(m, y), f = up == m ? 1.0f : ex2_approx(m - up);
+                        const float up = fmaxf(m, y - kLift<HALF>), f = up == m ? 1.0f : ex2_approx(m - up);
                         const float wt = in ? ex2_approx(y - up) : 0.0f;
                         m = up;
                         l = l * f + wt;
@@ -614,8 +613,8 @@ __device__ __forceinline__ bool attend(const TreeParams &p, WideShared &sh, uint
 #pragma unroll
                 for (int k = 0; k < 64; k += 2) top = fmax3(top, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
                 top *= scale;
-                if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                    const float up = fmaxf(top, m), f = up == m ? 1.0f : ex2_approx(m - up);
+                if (__any_sync(0xffffffffu, top > m + (kSlack + kLift<HALF>))) {
+                    const float up = fmaxf(top - kLift<HALF>, m), f = up == m ? 1.0f : ex2_approx(m - up);
                     m = up;
                     l *= f;
                     if (i > 0 || some_special) {  // else O is still zero

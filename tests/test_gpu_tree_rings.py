@@ -92,3 +92,37 @@ def test_odd_groups_in_every_tile_of_a_long_list(fmt, d, G, T):
     O, L = run_copies(fmt, d, G, T, S, lengths, D, C, MANY, edit=odd_groups(fmt, odd), seed=T)
     assert torch.isfinite(O[0, :, 0]).all() and torch.isfinite(L).all()
     assert torch.isfinite(O[:, :, 1, 32:]).all() and not torch.isfinite(O[:, :, 1, 3]).any()
+
+
+@pytest.mark.parametrize("T,copies", [(4, FEW), (8, FEW), (16, FEW), (20, MANY), (64, MANY)])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_many_light_keys_behind_a_heavy_one(fmt, T, copies):
+    """The nearest key takes the weight 1 and has values of zero, over a thousand others weigh
+    e^-17.8 = 2^-25.7 each with values of one: the output is their sum.  Weights that are rounded to
+    fp16 are so against 2^7 or more for the largest: to half of 2^-24 that is 2^-32 of the largest a
+    key, 1.3 % here; bf16 parts hold 16 bits of each."""
+    m = ssa()
+    S, d, ln = 1360, 64, 1280  # room for 64 nodes
+    D, C = [np.arange(1, 1250, dtype=np.int32)] * 2, [np.zeros(0, np.int32)] * 2
+    k, v = np.ones((1, 1, S, d)), np.ones((1, 1, S, d))
+    k[..., 1::2] = -1
+    k[:, :, ln - 1], v[:, :, ln - 1] = 2, 0
+    v[:, :, ln - 1, ::32] = 1  # no group of zeros
+    many = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev()).repeat(3 * copies, 1, 1, 1)
+    if fmt == "bf16":
+        cache = m.KVCache.from_tensors(many(k).bfloat16(), many(v).bfloat16())
+    else:
+        (kc, ks), (vc, vs) = R.encode(k, fmt), R.encode(v, fmt)
+        assert (R.decode(kc, ks, fmt) == k).all() and (R.decode(vc, vs, fmt) == v).all()
+        cache = m.KVCache.from_tensors(many(R.pack(kc, fmt)), many(R.pack(vc, fmt)), many(ks), many(vs), format=fmt)
+    lists = m.tree_lists(m.extend(*lists_to_device(D, C)[0], S), 1, depth=1)
+    q = torch.ones(3 * copies, T, 2, d, device=dev()).bfloat16()
+    par = torch.full((3 * copies, T), -1, device=dev(), dtype=torch.int32)
+    O, L = m.attn_tree(q, cache, torch.full((3 * copies,), ln, device=dev(), dtype=torch.int32), par, lists, scale=17.8 / 128)
+    n, w = 1248, np.exp(-17.8)
+    want = n * w / (1 + n * w)
+    slack = 2.0 ** -8 * want + (n * 2.0 ** -32 if fmt != "bf16" else 2.0 ** -16 * want) + 2.0 ** -17 * want
+    light = [e for e in range(d) if e % 32]
+    err = (O[..., light].double() - want).abs().max().item()
+    assert err <= slack, (err, slack)
+    assert (L.double() - (17.8 + np.log1p(n * w))).abs().max().item() <= 1e-5
