@@ -810,10 +810,10 @@ template <int D, int FMT, int ROWS>
 int launch_tree(TreeParams &p, int entries, cudaStream_t s) {
     using L = Layout<D, FMT, ROWS>;
     auto kernel = attn_tree_kernel<D, FMT, ROWS>;
+    int device = 0;
+    SSA_CUDA_TRY(cudaGetDevice(&device));
     if (L::kBytes > 40 * 1024) {  // once per device
         static std::atomic<uint64_t> done{0};
-        int device = 0;
-        SSA_CUDA_TRY(cudaGetDevice(&device));
         const uint64_t bit = device < 64 ? 1ull << device : 0;
         if (!(done.load() & bit)) {
             SSA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes));
@@ -825,8 +825,8 @@ int launch_tree(TreeParams &p, int entries, cudaStream_t s) {
     cfg.dynamicSmemBytes = L::kBytes;
     // Slices of the list: as many as run at once, with 64 keys each at least.  16 sequences x 8 KV
     // heads over 4400 e4m3 keys: 4 slices 44 us, 5, 6 and 8 slices (a second wave) 65, 59 and 57.
-    static std::atomic<int> clusters[kMaxSlices + 1];
-    p.slices = pick_slices(kernel, cfg, clusters, static_cast<long long>(p.B) * p.Hkv, entries / 64);
+    static ClusterCounts clusters;
+    p.slices = pick_slices(kernel, cfg, clusters, device, static_cast<long long>(p.B) * p.Hkv, entries / 64);
     cfg.gridDim = dim3(p.slices, p.Hkv, p.B);
     cfg.stream = s;
     cudaLaunchAttribute attr{};

@@ -4,9 +4,8 @@
 
 #include <cooperative_groups.h>
 
-#include <atomic>
-
 #include "kv_cache.cuh"
+#include "tree_launch.h"
 
 namespace ssa {
 
@@ -27,8 +26,6 @@ struct TreeParams {
 namespace {
 
 namespace cg = cooperative_groups;
-
-constexpr int kMaxSlices = 8;
 
 // Entries below x of a merged list: the rank of x's word and the bits under x.
 __device__ __forceinline__ int entries_below(const uint64_t *bits, const int32_t *rank, int x) {
@@ -382,29 +379,22 @@ struct LookUps {
     }
 };
 
-// The largest number of slices (CTAs of a cluster) with which `items` clusters run at once, at
-// most `most`; `cache` keeps the device's answers for the kernel (1 + clusters of k CTAs).
+// Slices of a launch of `items` problems, at most `most` each, by what the device runs at once.
 template <class Kernel>
-int pick_slices(Kernel kernel, cudaLaunchConfig_t cfg, std::atomic<int> (&cache)[kMaxSlices + 1], long long items, int most) {
-    for (int k = min(most, kMaxSlices); k > 1; --k) {
-        int n = cache[k].load();
-        if (n == 0) {
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = k;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            cfg.gridDim = dim3(k);
-            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-                cudaGetLastError();
-                n = 0;
-            }
-            cache[k].store(++n);
-        }
-        if (items <= n - 1) return k;
-    }
-    return 1;
+int pick_slices(Kernel kernel, cudaLaunchConfig_t cfg, ClusterCounts &counts, int device, long long items, int most) {
+    return pick_slices(counts, device, items, most, [&](int k) {
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = k;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3(k);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+        cudaGetLastError();
+        return -1;
+    });
 }
 
 // The problem of a CTA, but for the list lengths, and those.

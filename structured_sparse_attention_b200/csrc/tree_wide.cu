@@ -771,8 +771,8 @@ int launch(TreeParams &p, int rows, int entries, cudaStream_t s) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kBytes;
     // Slices of the list: as many as run at once, a tile each at least.
-    static std::atomic<int> clusters[kMaxSlices + 1];
-    p.slices = pick_slices(kernel, cfg, clusters, static_cast<long long>(p.B) * p.Hkv * row_blocks, (entries + kN - 1) / kN);
+    static ClusterCounts clusters;
+    p.slices = pick_slices(kernel, cfg, clusters, device, static_cast<long long>(p.B) * p.Hkv * row_blocks, (entries + kN - 1) / kN);
     cfg.gridDim = dim3(row_blocks * p.slices, p.Hkv, p.B);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
