@@ -252,7 +252,7 @@ struct Warp {
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
                     w[i] = pack_half(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-                const float down = scale_log2 * power_of_two(-up);
+                const float down = shifted_scale(scale_log2, up);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) scale[t][k] = __shfl_sync(0xffffffffu, down, (2 * q + k) * 4);
             }

@@ -498,6 +498,13 @@ __device__ __forceinline__ int query_shift(uint32_t top) { return min(14 - (stat
 
 __device__ __forceinline__ float power_of_two(int n) { return __uint_as_float(static_cast<uint32_t>(127 + n) << 23); }
 
+// Logit (log2 domain) per unit of the products of a query row shifted by `up`: not zero, with which
+// the -inf of a key that the row does not retain would be NaN (such products are under 2^38, so
+// that the logits are zero to fp32 either way).
+__device__ __forceinline__ float shifted_scale(float scale_log2, int up) {
+    return fmaxf(scale_log2 * power_of_two(-up), 1.17549435e-38f);
+}
+
 }  // namespace
 
 // KV heads of more rows than attn_tree_kernel takes (tree_wide.cu).

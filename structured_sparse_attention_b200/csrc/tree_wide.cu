@@ -333,7 +333,7 @@ __device__ __forceinline__ bool attend(const TreeParams &p, WideShared &sh, uint
             }
             const int up = query_shift(top);
             shift = power_of_two(up);
-            scale *= power_of_two(-up);
+            scale = shifted_scale(scale, up);
         }
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {

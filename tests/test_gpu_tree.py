@@ -665,3 +665,22 @@ def test_scale_bytes_out_of_range_are_reported(fmt, top, T):
             o, l = m.attn_tree(q, cache, length, par, lists, status=status, check=False)
             assert int(status) == -1 and torch.equal(o[1], O[1]) and torch.equal(l[1], L[1])
             t.copy_(keep)
+
+
+@pytest.mark.parametrize("fmt", R.FORMATS)
+@pytest.mark.parametrize("T", [2, 9, 40])
+def test_the_smallest_scales(fmt, T):
+    # scales whose product with a row's shift is below fp32: all logits are zero, masks still hold,
+    # and so do small groups
+    D, C = patterns(71, 2, 300, 60, 20)
+
+    def q_edit(q):
+        q[:, 0] *= 2.0 ** -60
+        q[:, 1] = 0
+
+    def edit(i, c, e=None):
+        if e is not None:
+            e[:, :, 200::40] = 100
+
+    for scale in (1e-37, 2.0 ** -100):
+        run(fmt, 64, 2, 1, 300, T, [250, 130], [T, T], D, C, 2, q_edit=q_edit, edit=edit, scale=scale)
