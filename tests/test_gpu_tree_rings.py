@@ -11,7 +11,7 @@ import torch
 
 import kv_ref as R
 from gpu_util import dev, lists_to_device, t_i32
-from test_gpu_tree import check, make_cache, random_tree, ssa
+from test_gpu_tree import check, make_cache, patterns, random_tree, run, ssa
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,45 @@ def test_many_light_keys_behind_a_heavy_one(fmt, T, copies):
     err = (O[..., light].double() - want).abs().max().item()
     assert err <= slack, (err, slack)
     assert (L.double() - (17.8 + np.log1p(n * w))).abs().max().item() <= 1e-5
+
+
+# every kernel at both head dimensions: 1 .. 8, 16 and 32 rows, blocks of 64 and 128 rows
+@pytest.mark.parametrize("G,T", [(1, 1), (3, 5), (4, 4), (1, 17), (2, 16), (4, 8), (3, 11), (4, 16), (5, 13), (2, 64), (8, 16),
+                                 (3, 43), (4, 64)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_row_counts_at_both_head_dimensions(fmt, d, G, T):
+    S = 400
+    D, C = patterns(G * 10 + T, 2 * G, S, 150, 40)
+    run(fmt, d, 2 * G, 2, S, T, [S - T, 130], [T, max(1, T - 3)], D, C, max(1, T // 2), seed=T + 1)
+
+
+# without odd groups: 4, 8, 16 and 32 rows, then 40, 128 and 150
+@pytest.mark.parametrize("G,T", [(4, 1), (2, 4), (4, 4), (2, 16), (2, 20), (2, 64), (3, 50)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_long_lists_on_one_cta(fmt, d, G, T):
+    S = 1300
+    D = [np.arange(7 * h, 1150 + 7 * h, dtype=np.int32) for h in range(G)]
+    C = [np.arange(h, S, 11, dtype=np.int32) for h in range(G)]
+    run_copies(fmt, d, G, T, S, [1230, 1001, 700], D, C, FEW if G * T <= 32 else MANY, seed=T + G)
+
+
+@pytest.mark.parametrize("G,T", [(2, 4), (2, 16), (2, 20), (3, 50)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_groups_that_are_not_finite_in_a_long_list(fmt, d, G, T):
+    # among groups of ordinary size: the kernel of many rows stays with fp16 tiles
+    S = 1300
+    D = [np.array([0], np.int32)] + [np.arange(1250, dtype=np.int32)] * (G - 1)
+    C = [np.arange(0, S - 100, 2, dtype=np.int32)] + [np.zeros(0, np.int32)] * (G - 1)
+    odd = np.arange(1, 1200, 16)
+
+    def edit(i, c, e):
+        if i == 1:
+            c[:, :, odd, :32] = 0
+            e[:, :, odd, 0] = 255
+
+    O, L = run_copies(fmt, d, G, T, S, [1230, 1001, 700], D, C, FEW if G * T <= 32 else MANY, edit=edit, seed=T)
+    assert torch.isfinite(O[0, :, 0]).all() and torch.isfinite(L).all()
+    assert torch.isfinite(O[:, :, 1, 32:]).all() and torch.isnan(O[:, :, 1, :32]).all()
