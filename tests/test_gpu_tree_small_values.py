@@ -131,3 +131,62 @@ def test_small_groups_are_as_fast_many_rows(fmt, T, edit):
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_a_small_group_at_the_end_of_a_list(fmt, T):
     assert time_ratio(fmt, 128, T, last_column) <= 2.5
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_waits_run_out_in_a_list_that_is_taken_again(fmt):
+    # with the limit at 0 some wait of the first or of the second pass gives up; the same context
+    # then runs a normal call
+    m = ssa()
+    S, T, d = 300, 40, 64
+    D, C = patterns(51, 4, S, 150, 30)
+    lists = m.tree_lists(m.extend(*lists_to_device(D, C)[0], S), 2, depth=T)
+    g = torch.Generator(device=dev()).manual_seed(5)
+    rand = lambda *n: torch.randn(*n, device=dev(), generator=g).bfloat16()
+    cache = m.KVCache(2, 2, S, d, fmt, device=dev())
+    m.kv_append(cache, rand(2 * S, 2, d), rand(2 * S, 2, d), t_i32([0, S, 2 * S]), t_i32([0, 0]))
+    cache.v_scale[0] -= 16
+    q, length = rand(2, T, 4, d), t_i32([200, 200])
+    want = [x.clone() for x in m.attn_tree(q, cache, length, None, lists)]
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    old = m.set_wait_limit_ns(0)
+    try:
+        m.attn_tree(q, cache, length, None, lists, status=status, check=False)
+        torch.cuda.synchronize()
+    finally:
+        m.set_wait_limit_ns(old)
+    assert int(status) == -5
+    for x, y in zip(m.attn_tree(q, cache, length, None, lists), want):
+        assert torch.equal(x, y)
+
+
+def test_a_list_taken_again_repeats_in_a_graph():
+    # small groups in one of two sequences, other calls in flight on another stream
+    m = ssa()
+    S, T, d, Hq, Hkv = 2000, 40, 128, 8, 2
+    D, C = [np.arange(700, dtype=np.int32)] * Hq, [np.arange(0, S, 17, dtype=np.int32)] * Hq
+    lists = m.tree_lists(m.extend(*lists_to_device(D, C)[0], S), Hkv, depth=T)
+    g = torch.Generator(device=dev()).manual_seed(6)
+    rand = lambda *n: torch.randn(*n, device=dev(), generator=g).bfloat16()
+    cache = m.KVCache(2, Hkv, S, d, "e4m3", device=dev())
+    m.kv_append(cache, rand(2 * S, Hkv, d), rand(2 * S, Hkv, d), t_i32([0, S, 2 * S]), t_i32([0, 0]))
+    cache.v_scale[1, :, 1000:] -= 16
+    q, length = rand(2, T, Hq, d), t_i32([1900, 1900])
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    outs = [(torch.zeros_like(q), torch.zeros(2, T, Hq, device=dev())) for _ in range(3)]
+    call = lambda o: m.attn_tree(q, cache, length, None, lists, out=o[0], lse=o[1], status=status, check=False)
+    call(outs[0])
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, o in zip(graphs, outs[1:]):
+        with torch.cuda.graph(graph):
+            call(o)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert int(status) == 0 and outs[0][0].abs().sum() > 0
+    for o in outs[1:]:
+        assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
