@@ -742,7 +742,8 @@ def attn_tree(q, cache: KVCache, length, parent, lists: TreeLists, *, n_nodes=No
 
     q [B, T, H_q, d] bf16; length [B] int32 committed rows, the nodes' keys and values in the
     rows length + n; parent [B, T] int32 (None: a chain), n_nodes [B] int32 (None: T each).
-    T = 1 is the ordinary decoding step.  Returns (O [B, T, H_q, d] bf16, LSE [B, T, H_q] fp32);
+    T = 1 is the ordinary decoding step (attn_decode does it too over a bf16 cache, and faster for one
+    to four sequences whose heads share no keys).  Returns (O [B, T, H_q, d] bf16, LSE [B, T, H_q] fp32);
     rows of nodes >= n_nodes[b] are left as they were (0 and -inf in outputs made here)."""
     lib = load()
     dev = cache.device

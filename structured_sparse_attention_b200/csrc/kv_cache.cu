@@ -4,7 +4,7 @@
 //                     position rotation, rounding to the cache's format, in one pass
 //   kv_read_kernel    cache rows back to bf16
 //
-// Both are bound by the bytes they move; the design keeps every access a full 16 (8, 4)
+// The bytes they move are most of the work; the design keeps every access a full 16 (8, 4)
 // bytes a lane over whole rows and computes a token's angles once for many heads.
 #include "kv_cache.cuh"
 #include "trace.h"
@@ -241,10 +241,11 @@ __device__ __forceinline__ void sincos_turn(double turn, float &s, float &c) {
 // cp.async into slots of its own in shared memory, kAhead rows ahead: what is in flight
 // takes no registers and needs no barrier.  Arithmetic is on packed pairs.
 //
-// 16384 tokens of 32 + 2 x 8 heads, d = 64, to e4m3 with k_out and v_out: 49 us, 4.5 TB/s moved,
-// 68 % of the card's copy rate; over half of its bytes are writes, which memory alone takes at
-// 3.9 TB/s.  Two CTAs of 106 registers a thread leave 4 warps a scheduler, which issue in half of
-// the cycles.  With a register prefetch of the rows in place of cp.async it took 66 us.
+// 16384 tokens of 32 + 2 x 8 heads, d = 64, with k_out and v_out: to e4m3 49 us, 4.5 TB/s moved, 68 %
+// of the card's copy rate; to bf16 47 us, 5.0 TB/s; to e2m1 50 us, 4.2 TB/s.  Nothing is full: DRAM is
+// active 41 % of the time and the schedulers issue in half of the cycles, with the 4 warps each
+// that two CTAs of 106 registers a thread leave; 768 CTAs on 296 places are 2.6 waves.  With a
+// register prefetch of the rows in place of cp.async it took 66 us.
 constexpr int kAhead = 4;
 
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
@@ -392,10 +393,11 @@ struct ReadParams {
 // A lane decodes 8 elements (one 16-byte store) of each of kReadAhead tokens, whose loads are all
 // under way before the first is used; a CTA takes one head of the keys or of the values.
 //
-// Bound by memory, by its writes: 2 bytes an element against 1.03 (e4m3) or 0.53 (e2m1) read.
-// 65536 e4m3 tokens of 8 heads, d = 128: 71 us, 5.7 TB/s moved, 87 % of the card's copy rate;
-// 3 x 104000 e2m1 tokens: 340 us, 4.6 TB/s moved, of which the writes 3.6 TB/s, where a fill of
-// memory alone reaches 3.9.
+// 65536 tokens of 8 heads, d = 128: bf16 80 us, 6.7 TB/s moved; e4m3 65 us, 6.3 TB/s, 96 % of the card's
+// copy rate; e2m1 71 us, 4.8 TB/s.  bf16 and e4m3 are bound by memory.  e2m1 is bound by
+// instructions: 3 x 104000 tokens take 340 us, 4.0 TB/s moved (3.2 of them writes, where a fill of
+// memory reaches 4.0), with 84 % of the issue slots full: the descriptor search of each lane and
+// token and the decoding, for 16 bytes written.
 constexpr int kReadAhead = 4;
 
 template <int D, int FMT>
@@ -523,7 +525,7 @@ extern "C" int sparse_kv_append(const ssa_kv_cache *cache, const ssa_kv_append_a
     p.Hkv = cache->H_kv;
     // Rows a unit takes: as many as leave 32 warps for each SM (a token's angles are then
     // computed once for up to 16 rows), one where there are few tokens.  With 1 and 16 rows:
-    // 16 x 13 tokens of 32 + 2 x 8 heads 5.2 and 16.0 us, 16384 tokens 112 and 49 us.
+    // 16 sequences of up to 13 tokens (118) of 32 + 2 x 8 heads 5.2 and 16.0 us, 16384 tokens 112 and 49 us.
     const int HT = p.Hq + 2 * p.Hkv;
     p.chunk = 16;
     while (p.chunk > 1 && static_cast<long long>(p.n_pad) * ((HT + p.chunk - 1) / p.chunk) / per_warp < 148 * 32)

@@ -29,12 +29,12 @@
 // no workspace and repeats bit for bit.
 //
 // Measured, d = 128: 16 sequences of 16384 rows, 32 query heads on 8, one token, e4m3, lists
-// of about 4400 keys: 43.1 us, 3.4 TB/s of codes and scales gathered, 53 % of the card's copy
-// rate.  DRAM runs at 42 % of its peak and the schedulers issue in 39 % of the cycles: with 128
+// of about 4400 keys: 44 us, 3.4 TB/s of codes and scales gathered, 52 % of the card's copy
+// rate.  DRAM runs at 41 % of its peak and the schedulers issue in 39 % of the cycles: with 128
 // registers a thread an SM holds 16 of these warps, which wait in turn for their gathers
-// (stalls 1.3 an issued instruction), for their own arithmetic (1.4) and for shared memory
-// (1.0); and 512 CTAs leave 14 % of the places for 592 empty.  One sequence, bf16, 1-token
-// step: 8.6 us, a chain of a launch, the lists, the look-ups, a gather and the join.
+// (stalls 1.2 an issued instruction), for their own arithmetic (1.5) and for shared memory
+// (0.7); and 512 CTAs leave 14 % of the places for 592 empty.  One sequence, bf16, 1-token
+// step: 8.8 us, a chain of a launch, the lists, the look-ups, a gather and the join.
 #include <atomic>
 #include <type_traits>
 

@@ -36,10 +36,11 @@
 // instruction caches, not for the units.
 //
 // Measured, d = 128: 16 trees of 64 nodes, 32 query heads on 8, e4m3, lists of about 1000 keys:
-// 60.7 us.  The products alone would take 7 us at the card's bf16 rate (tensor pipe 8.5 % busy);
-// a tile takes 2500 to 3000 cycles, most of them the softmax of 64 keys a row by one warp a
-// scheduler (a sixth of the working warps' stalls wait for instructions to be fetched), and 256
-// CTAs on 148 SMs make two waves.  4 trees of 16 nodes over 104000 rows, bf16: 54 us.
+// 62 us.  The tiles' products alone, masked pairs included, would take 7 us at the card's bf16 rate
+// (tensor pipe 8 % busy); a tile takes 2500 to 3000 cycles, most of them the softmax of 64 keys a
+// row by one warp a scheduler (a sixth of the working warps' stalls wait for instructions to be
+// fetched), and 256 CTAs on 148 SMs make two waves.  4 trees of 16 nodes over 104000 rows, bf16:
+// 55 us.
 #include <atomic>
 
 #include "trace.h"
